@@ -75,8 +75,12 @@ struct Shared {
   uint32_t n_list;
 };
 
-constexpr size_t kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
-static_assert(kSharedBytes + sizeof(float) * kThreads * (kMaxListed + 8) <= 227 * 1024, "shared memory");
+// With room for `listed` keys per thread, and the `v` that a step may write behind them.
+constexpr size_t shared_bytes(int listed, int v) {
+  return (sizeof(Shared) + 15) / 16 * 16 + sizeof(float) * kThreads * (listed + v);
+}
+constexpr size_t kSharedBytes = shared_bytes(0, 0);
+static_assert(shared_bytes(kMaxListed, 8) <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) { return mapa_shared(smem_u32(p), rank); }
 
@@ -1279,8 +1283,11 @@ cudaError_t launch_sample(const uw_sample_args& a, int sms, cudaStream_t s) {
   // that: what is left of the SM's memory is the cache that holds loads in flight.
   // 256 rows of 100 003 without a draw took 29 us with 38, 24 with this.)
   p.listed = std::min(kMaxListed, std::max(16, p.run / (3 * kThreads)));
-  const size_t smem = kSharedBytes + sizeof(float) * kThreads * (p.listed + Row<T>::V);
-  const cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = shared_bytes(p.listed, Row<T>::V);
+  // The limit belongs to the kernel and the device, not to this call: it is always set to the most that
+  // any call needs, so that no other thread's call lowers it between here and the launch.
+  const cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)shared_bytes(kMaxListed, Row<T>::V));
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(sample_kernel<T>, dim3((unsigned)(a.n_rows * c)), c, dim3(kThreads), smem, s, p);
 }
