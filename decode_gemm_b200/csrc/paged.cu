@@ -68,6 +68,7 @@ using namespace sm100;
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxRequests = 8192;
+constexpr size_t plan_shared_bytes(int requests) { return ((size_t)4 * requests + 2) * 4; }
 
 struct PlanParams {
   uw_paged_plan_args a;
@@ -453,10 +454,12 @@ uw_status uw_paged_plan(const uw_paged_plan_args* a, void* stream) {
   // one CTA while a few rows per thread are all there is (no barrier between
   // CTAs then), else the eight of the largest portable cluster
   const int cluster = a->n_rows <= 4 * kPlanThreads && a->n_requests <= 4 * kPlanThreads ? 1 : 8;
-  const size_t smem = ((size_t)4 * a->n_requests + 2) * 4;
+  const size_t smem = plan_shared_bytes(a->n_requests);
+  // (the limit is the kernel's, not this call's: set to the most that any call needs, so that no other
+  // thread's call lowers it before the launch)
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess)
+      cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)plan_shared_bytes(kPlanMaxRequests)) != cudaSuccess)
     return map_launch(cudaGetLastError());
   return map_launch(launch_pdl_cluster(paged_plan_kernel, dim3(cluster), cluster, dim3(kPlanThreads), smem,
                                        static_cast<cudaStream_t>(stream), p));

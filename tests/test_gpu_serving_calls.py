@@ -62,3 +62,32 @@ def test_sample_from_several_host_threads(uw):
     for _, _, ids, x, *_ in cases:
         at = torch.arange(x.shape[1], device="cuda")
         assert torch.equal(ids, torch.where(x == x.amax(1, keepdim=True), at, x.shape[1]).amin(1))
+
+
+def _plan_tensors(n):
+    """One new token for each of n requests that store one already, as a uw_paged_plan_args."""
+    import torch
+    t = {k: torch.full((m,), v, dtype=d, device="cuda") for k, m, v, d in (
+        ("ctx", n, 1, torch.int32), ("new", n, 1, torch.int32), ("head", 1, -7, torch.int32), ("table", n, 5, torch.int32),
+        ("cu", n + 1, -7, torch.int32), ("kv", n, -7, torch.int32), ("pos", n, -7, torch.int32), ("slots", n, -7, torch.int64))}
+    p = {k: v.data_ptr() for k, v in t.items()}
+    return t, lambda uw: uw.uw_paged_plan_args(p["ctx"], p["new"], None, None, p["head"], p["table"], p["cu"], p["kv"],
+                                               p["pos"], p["slots"], None, 1, n, n, 1, 0, 8)
+
+
+def _plan_is_right(t, n):
+    assert t["cu"].tolist() == list(range(n + 1)) and t["kv"].tolist() == [2] * n and t["head"].tolist() == [0]
+    assert t["pos"].tolist() == [1] * n and t["slots"].tolist() == [5 * 8 + 1] * n
+
+
+def test_plan_from_several_host_threads(uw):
+    """Numbers of requests whose launches need different amounts of shared memory, on a stream each."""
+    import torch
+    cases = [(n, *_plan_tensors(n), torch.cuda.Stream()) for n in (8192, 3500, 7000, 4000)]
+    torch.cuda.synchronize()
+    seen = _at_once(*(lambda a=args(uw), s=s: uw.lib.uw_paged_plan(C.byref(a), s.cuda_stream) for _, _, args, s in cases),
+                    times=5000)
+    torch.cuda.synchronize()
+    assert seen == {uw.UW_OK}
+    for n, t, *_ in cases:
+        _plan_is_right(t, n)
