@@ -455,9 +455,10 @@ uw_status uw_paged_plan(const uw_paged_plan_args* a, void* stream) {
   // CTAs then), else the eight of the largest portable cluster
   const int cluster = a->n_rows <= 4 * kPlanThreads && a->n_requests <= 4 * kPlanThreads ? 1 : 8;
   const size_t smem = plan_shared_bytes(a->n_requests);
-  // (the limit is the kernel's, not this call's: set to the most that any call needs, so that no other
-  // thread's call lowers it before the launch)
-  if (smem > 48 * 1024 &&
+  // (The limit is the kernel's, not this call's: set to the most that any call needs, so that no other
+  // thread's call lowers it before the launch.  Without it 48 KB are the limit of this and of the kernel's
+  // own arrays together; half of that leaves them room.)
+  if (smem > 24 * 1024 &&
       cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)plan_shared_bytes(kPlanMaxRequests)) != cudaSuccess)
     return map_launch(cudaGetLastError());

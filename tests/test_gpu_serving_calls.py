@@ -91,3 +91,39 @@ def test_plan_from_several_host_threads(uw):
     assert seen == {uw.UW_OK}
     for n, t, *_ in cases:
         _plan_is_right(t, n)
+
+
+def _in_a_process(body):
+    """Run `body` in a process that has launched nothing else before (limits and switches are per process)."""
+    head = f"""
+        import sys
+        sys.path.insert(0, {ROOT!r})
+        from tests import test_gpu_serving_calls as t
+        import numpy as np
+        import torch
+        import decode_gemm_b200 as uw
+    """
+    return textwrap.dedent(head) + textwrap.dedent(body)
+
+
+def _run(code, **env):
+    r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, **env), capture_output=True, text=True, timeout=300,
+                       cwd=ROOT)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+def test_plan_around_the_shared_memory_that_needs_no_limit(uw):
+    """From a few thousand requests on, a launch needs a raised limit; what the kernel holds beside the requests'
+    numbers counts too.  Rising numbers in a process of its own, where no larger call has raised it."""
+    out = _run(_in_a_process("""
+        import ctypes as C
+        for n in (3000, 3054, 3055, 3056, 3057, 3063, 3070, 3071, 3080):
+            tensors, args = t._plan_tensors(n)
+            status = uw.lib.uw_paged_plan(C.byref(args(uw)), None)
+            assert status == uw.UW_OK, (n, status)
+            torch.cuda.synchronize()
+            t._plan_is_right(tensors, n)
+        print("all planned")
+    """))
+    assert "all planned" in out
