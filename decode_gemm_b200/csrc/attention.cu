@@ -24,13 +24,15 @@
 //   * Warps: 0-3 and 4-7 softmax of stream 0 and 1 (a thread per row), 8 loads Q and K,
 //     11 loads V, 9 issues the products, 10 walks the CTA's share and hands out units.
 //   * Every wait is bounded; on expiry the kernel raises UW_FLAG_TIMEOUT, waits
-//     for its copies and products in flight, frees TMEM and returns.
+//     for its copies and products in flight (once all warps have stopped: one that
+//     was through before the expiry has left some too), frees TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <mutex>
 
 #include "attention_sm100.cuh"
@@ -81,6 +83,7 @@ struct AttnParams {
   float scale_log2;         // |scale| * log2(e)
   int32_t turn;             // scale <= 0: scores are taken as (x & s_and) ^ s_xor
   uint32_t s_and, s_xor;
+  int32_t withhold;         // failure-detection tests: the second row tile's last signal stays away
   uint64_t wait_ns;
 };
 
@@ -224,6 +227,13 @@ struct FewRows {
     tmem_st_wait();
   }
 };
+
+// All warps are through their work: `abort` keeps its value from here on.  (A barrier of its own, since the
+// warps come to it from different places.)
+__device__ __forceinline__ void work_ends() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 
 // log sum of exponentials, from base-two maximum and sum.
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -511,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         }
         reinterpret_cast<JoinRecord*>(a.ws_dev)[cta] = rec;
       }
-      __syncwarp();
+      work_ends();
     } else if (warp == kLoadWarp || warp == kLoadVWarp) {
       // One warp loads Q and K, the other V.  A lane per box of the tile: its
       // page's id is fetched a tile ahead, and each lane issues its own copies,
@@ -589,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         rank += 2 * u.n_tiles;
       }
       if (bad && a.flags_dev) atomicOr(a.flags_dev, (uint32_t)UW_FLAG_BAD_INPUT);
+      work_ends();
       if (*abort && lane == 0) {  // leave no copy in flight
         // (a buffer's phase that this warp did not fill is over or never began;
         // the wait for it is bounded like every other)
@@ -677,12 +688,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
           ++weights[s];
           tc_fence_after();
           output(s, v, i < 2, !two || s == 1);
-          if (i + 2 >= steps) mma_commit_elect(bar(L::bOut + s));
-          else score(s, two ? (i + 2) >> 1 : i + 2, k, !two || s == 1);
+          if (i + 2 >= steps) {
+            if (!(p.withhold && two && s == 1)) mma_commit_elect(bar(L::bOut + s));
+          } else score(s, two ? (i + 2) >> 1 : i + 2, k, !two || s == 1);
         }
         ++pieces;
       }
-      __syncwarp();
+      work_ends();
       if (*abort) {  // leave no product in flight
         volatile int none = 0;
         mma_commit_elect(bar(L::bDrain));
@@ -903,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
       }
       ++n;
     }
-    __syncwarp();
+    work_ends();
   }
   tc_fence_before();
   __syncthreads();
@@ -1127,6 +1139,10 @@ uw_status uw_paged_attention(const uw_paged_attention_args* a, void* stream) {
   }
   if (!windowed) p.a.window = 0;
   p.wait_ns = wait_limit_ns();
+  // Failure-detection tests (the GEMM's switch, read once per process): units of two row tiles never signal
+  // the second one's outputs, so that waits run out; single tokens go on as ever.
+  static const int withhold = std::getenv("UW_TEST_WITHHOLD_HANDOFF") ? 1 : 0;
+  p.withhold = withhold;
   if (!make_q_map(&p.q, *a, p.group, p.per_tile) || !make_q_map(&p.q_one, *a, p.group, 1) ||
       !make_map(&p.k, a->cache.k_dev, a->cache) ||
       !make_map(&p.v, a->cache.v_dev, a->cache))

@@ -127,3 +127,26 @@ def test_plan_around_the_shared_memory_that_needs_no_limit(uw):
         print("all planned")
     """))
     assert "all planned" in out
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (8, 8, 64)])
+def test_attention_bounded_wait_reports_timeout(uw, heads, kv_heads, dim):
+    """A wait on a signal that nothing gives runs out (100 ms here): the call raises UW_FLAG_TIMEOUT and returns, and
+    the same process goes on attending.  The switch keeps back the last signal of units of two row tiles, so
+    prompts run out and single tokens do not; it is read once per process, hence a process of its own."""
+    out = _run(_in_a_process(f"""
+        import time
+        from tests import test_gpu_serving as g
+        shape = ({heads}, {kv_heads}, {dim})
+        prompts = g._requests(g._gen(1), np.random.default_rng(1), [(900, 700), (1500, 40), (800, 800), (64, 1)], 16, *shape)
+        tokens = g._requests(g._gen(2), np.random.default_rng(2), [(300, 1), (1, 1), (0, 0), (2000, 1)], 16, *shape)
+        for _ in range(3):
+            began = time.monotonic()
+            out, lse, flags = g._attend(uw, *prompts)
+            assert flags == uw.UW_FLAG_TIMEOUT, flags
+            assert time.monotonic() - began < 20
+            assert bool((out[-3:] == 77).all()) and bool((lse[-3:] == 77).all())  # rows of no request
+            g._check_attention(uw, *tokens)
+        print("timeout reported, attention usable")
+    """), UW_TEST_WITHHOLD_HANDOFF="1", UW_WAIT_LIMIT_MS="100")
+    assert "timeout reported, attention usable" in out
