@@ -246,9 +246,9 @@ struct Request {
 };
 
 __device__ __forceinline__ Request request_of(const AttnParams& p, int b, bool* bad) {
-  const int64_t rows = p.a.n_rows;
-  const int64_t c0 = min(max((int64_t)__ldg(p.a.cu_q_dev + b), (int64_t)0), rows);
-  const int64_t c1 = min(max((int64_t)__ldg(p.a.cu_q_dev + b + 1), c0), rows);
+  const int64_t rows = p.a.n_rows, from = __ldg(p.a.cu_q_dev + b), to = __ldg(p.a.cu_q_dev + b + 1);
+  if (from < 0 || to < from || to > rows) *bad = true;
+  const int64_t c0 = min(max(from, (int64_t)0), rows), c1 = min(max(to, c0), rows);
   const int64_t most = min((int64_t)p.a.table_width << p.page_shift, (int64_t)INT32_MAX - 2 * kKeys);
   const int64_t kv = __ldg(p.a.kv_len_dev + b);
   if (c1 > c0 && (kv < 0 || kv > most)) *bad = true;

@@ -561,8 +561,9 @@ typedef struct uw_paged_attention_args {
  * lse = log sum_j exp(s_j).
  *   - A row that sees nothing (p < 0) gets out = 0 and lse = -infinity.
  *   - Rows behind cu_q[n_requests] and rows of no request are left as they
- *     were.  cu_q is cut to 0..n_rows, and kv_len to 0..table_width *
- *     page_size with UW_FLAG_BAD_INPUT.
+ *     were.  cu_q is cut to 0..n_rows and kv_len to 0..table_width * page_size,
+ *     with UW_FLAG_BAD_INPUT.  A cu_q that falls raises it too; rows that it
+ *     gives to two requests are unspecified.
  *   - Neither keys nor values at positions that no row of the request sees
  *     matter, whatever they hold; pages outside them are not read (their table
  *     entries may be anything).  Page ids outside 0..n_pages - 1 in the others

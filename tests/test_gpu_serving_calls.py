@@ -150,3 +150,20 @@ def test_attention_bounded_wait_reports_timeout(uw, heads, kv_heads, dim):
         print("timeout reported, attention usable")
     """), UW_TEST_WITHHOLD_HANDOFF="1", UW_WAIT_LIMIT_MS="100")
     assert "timeout reported, attention usable" in out
+
+
+def test_attention_reports_row_offsets_out_of_order(uw):
+    """cu_q below zero, beyond the rows, or falling: reported, cut, and never followed."""
+    from tests import test_gpu_serving as g
+    gen, rng = g._gen(10), np.random.default_rng(10)
+    q, kc, vc, table, cu, kv = g._requests(gen, rng, [(200, 2), (90, 1), (40, 40)], 16, 4, 2, 64)
+    good, _, flag = g._attend(uw, q, kc, vc, table, cu, kv)
+    assert flag == 0 and list(cu) == [0, 2, 3, 43] and q.shape[0] == 46
+    for bad, sound in (([0, 2, 3, 47], 3), ([0, 2, 3, 2**31 - 1], 3), ([0, 2, 3, -2**31], 3), ([0, 2, 1, 1], 1),
+                       ([-1, 2, 3, 43], 0), ([46, 46, 46, 45], 0)):
+        out, _, flag = g._attend(uw, q, kc, vc, table, bad, kv)
+        assert flag == uw.UW_FLAG_BAD_INPUT, bad
+        assert np.array_equal(g._f64(out)[:sound], g._f64(good)[:sound]), bad
+    # as far as the rows go, and requests without rows at their end: sound
+    for fine in ([0, 2, 3, 46], [0, 2, 3, 3], [46, 46, 46, 46], [0, 0, 0, 0]):
+        assert g._attend(uw, q, kc, vc, table, fine, kv)[2] == 0, fine
