@@ -638,7 +638,11 @@ def _cache_fields(call, dev, k, v, dim):
     return k.data_ptr(), v.data_ptr(), shape[0], strides[0], strides[1], strides[2], shape[1], shape[2], dim, 0
 
 
-def _serve(fn, name, dev, args, stream):
+def _serve(fn, name, dev, pack, fields, stream):
+    try:
+        args = pack(*fields)
+    except struct.error as e:  # (a number that its field cannot hold)
+        raise UwError(UW_ERR_ARG, f"{name}: {e}") from None
     if stream is None:
         stream = _raw_stream(dev) if dev >= 0 else 0
     else:
@@ -660,7 +664,7 @@ def uw_paged_plan(ctx_len, new_len, page_size: int, free_pages, table, cu_q, kv_
         (head_in, "head_in", i32, 1), (head_out, "head_out", i32, 1), (cu_q, "cu_q", i32, n + 1),
         (kv_len, "kv_len", i32, n), (positions, "positions", i32, rows),
         (slots, "slots", _TYPES["i64"], rows), (flags, "flags", _TYPES["u32"], 1)))
-    _serve(_plan_fn, f, dev, _PACK_PLAN(*ptr[:5], at, *ptr[5:], apart, rows, n, width, spare, page_size), stream)
+    _serve(_plan_fn, f, dev, _PACK_PLAN, (*ptr[:5], at, *ptr[5:], apart, rows, n, width, spare, page_size), stream)
 
 
 def uw_qk_norm_rope(q, k, v, positions, inv_freq, slots, k_cache, v_cache, q_out, q_weight=None,
@@ -684,8 +688,8 @@ def uw_qk_norm_rope(q, k, v, positions, inv_freq, slots, k_cache, v_cache, q_out
         (q_weight, "q_weight", bf16, dim), (k_weight, "k_weight", bf16, dim),
         (positions, "positions", _TYPES["i32"], rows), (inv_freq, "inv_freq", _TYPES["f32"], half),
         (slots, "slots", _TYPES["i64"], rows), (flags, "flags", _TYPES["u32"], 1)))
-    _serve(_rope_fn, f, dev, _PACK_ROPE(qp, kp, vp, wq, wk, pos, inv, at, op, flag, *cache, rows, qs, ks, vs, os_,
-                                        heads, 2 * half, 1 if interleaved else 0, eps), stream)
+    _serve(_rope_fn, f, dev, _PACK_ROPE, (qp, kp, vp, wq, wk, pos, inv, at, op, flag, *cache, rows, qs, ks, vs, os_,
+                                          heads, 2 * half, 1 if interleaved else 0, eps), stream)
 
 
 def uw_paged_attention_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -712,7 +716,7 @@ def uw_paged_attention(q, k_cache, v_cache, table, cu_q, kv_len, out, scale: flo
     cu, kv, lp, flag, wp = _vectors(f, dev, (
         (cu_q, "cu_q", i32, n + 1), (kv_len, "kv_len", i32, n), (lse, "lse", _TYPES["f32"], rows * heads),
         (flags, "flags", _TYPES["u32"], 1), (ws, "ws", _TYPES["u8"], ws_bytes)))
-    _serve(_attention_fn, f, dev, _PACK_ATTENTION(
+    _serve(_attention_fn, f, dev, _PACK_ATTENTION, (
         qp, tp, cu, kv, op, lp, flag, wp, *_cache_fields(f, dev, k_cache, v_cache, dim), ws_bytes, rows, qs, os_, ts,
         n, width, heads, window, 0 if out.dtype in bf16 else 1, dim ** -0.5 if scale is None else scale), stream)
 
@@ -730,7 +734,7 @@ def uw_sample(logits, u, ids, temperature=None, top_k=None, top_p=None, min_p=No
     ptr = _vectors(f, dev, (
         (u, "u", f32, n), (temperature, "temperature", f32, n), (top_k, "top_k", _TYPES["i32"], n),
         (top_p, "top_p", f32, n), (min_p, "min_p", f32, n), (ids, "ids", _TYPES["i64"], n), (prob, "prob", f32, n)))
-    _serve(_sample_fn, f, dev, _PACK_SAMPLE(at, *ptr, n, apart, vocab, 0 if logits.dtype in f32 else 1), stream)
+    _serve(_sample_fn, f, dev, _PACK_SAMPLE, (at, *ptr, n, apart, vocab, 0 if logits.dtype in f32 else 1), stream)
 
 
 # the same entry points, taking the packed bytes of their argument structure
