@@ -630,10 +630,12 @@ def _cache_fields(call, dev, k, v, dim):
     kinds, shape = _TYPES["bf16"], k.shape
     if len(shape) != 4 or shape[3] != dim:
         raise UwError(UW_ERR_SHAPE, f"{call}: k_cache is {tuple(shape)}, not (pages, page_size, heads, {dim})")
-    strides = k.stride()
+    strides, of_v = k.stride(), v.stride()
+    if 1 in shape and v.shape == shape:  # (no stride of an axis of one entry means anything: the same for both)
+        strides, of_v = ([dim if n == 1 else s for n, s in zip(shape[:3], t)] + [t[3]] for t in (strides, of_v))
     if k.dtype not in kinds or k.get_device() != dev or (strides[3] != 1 and dim > 1):
         _refuse(call, dev, k, "k_cache", kinds, shape)
-    if v.dtype not in kinds or v.get_device() != dev or v.shape != shape or v.stride() != strides:
+    if v.dtype not in kinds or v.get_device() != dev or v.shape != shape or of_v != strides:
         _refuse(call, dev, v, "v_cache", kinds, shape)
     return k.data_ptr(), v.data_ptr(), shape[0], strides[0], strides[1], strides[2], shape[1], shape[2], dim, 0
 

@@ -44,3 +44,36 @@ def test_numbers_that_their_fields_cannot_hold(uw):
         with pytest.raises(uw.UwError, match=name) as e:
             call(uw, **over)
         assert e.value.status == uw.UW_ERR_ARG, over
+
+
+def _cache_that_is_passed_on(uw, monkeypatch, call, fn, args, **over):
+    kept = []
+    monkeypatch.setattr(uw, fn, lambda packed, stream: kept.append(packed) or 0)
+    call(uw, **over)
+    return getattr(uw, args).from_buffer_copy(kept[0].ljust(128 * 4, b"\0")).cache
+
+
+@pytest.mark.parametrize("fn,args", [("_rope_fn", "uw_qk_norm_rope_args"), ("_attention_fn", "uw_paged_attention_args")])
+@pytest.mark.parametrize("axis", [0, 1, 2])
+def test_caches_with_an_axis_of_one_entry(uw, monkeypatch, fn, args, axis):
+    """The stride of such an axis is never stepped along: whatever it is, and whether or not keys and values
+    have the same one, the cache is the same."""
+    call, shape = (_rope if fn == "_rope_fn" else _attend), [3, 8, 2, 64]
+    shape[axis] = 1
+    over = dict(k=_zeros(2, shape[2], 64, t="bfloat16"), v=_zeros(2, shape[2], 64, t="bfloat16")) if call is _rope else {}
+    plain = _zeros(*shape, t="bfloat16")
+    for odd in (0, 1, 3, 10**12):
+        strides = list(plain.stride())
+        strides[axis] = odd
+        other = plain.as_strided(shape, strides)
+        for k, v in ((other, plain), (plain, other), (other, other)):
+            c = _cache_that_is_passed_on(uw, monkeypatch, call, fn, args, k_cache=k, v_cache=v, **over)
+            got = [c.page_stride, c.slot_stride, c.head_stride]
+            assert [g for i, g in enumerate(got) if i != axis] == [g for i, g in enumerate(plain.stride()[:3]) if i != axis]
+            assert got[axis] > 0 and got[axis] % 8 == 0 and got[axis] < 2**39
+            assert [c.n_pages, c.page_size, c.n_kv_heads, c.head_dim] == shape
+    # axes that are stepped along have to agree
+    wide = _zeros(*[n + (n > 1) for n in shape[:3]], 64, t="bfloat16")[:shape[0], :shape[1], :shape[2]]
+    with pytest.raises(uw.UwError) as e:
+        call(uw, k_cache=plain, v_cache=wide, **over)
+    assert e.value.status == uw.UW_ERR_ARG
