@@ -127,7 +127,8 @@ __device__ __forceinline__ uint32_t least_key(uint32_t lo, uint32_t hi, F fits) 
   return hi;
 }
 
-// One row's weights: w(x) = 2^40 e^((x - max) / t), to about 2^-32 of itself.
+// One row's weights: w(x) = 2^40 e^((x - max) / t), to 2^-29.8 of itself (2^-31.7 in the mean of squares: a table
+// entry and a correction, each rounded to a unit of a number of 31 bits), the bits below one dropped.
 // y = (max - x) log2(e) / t = i / 512 + g with g small, and the weight is a table
 // entry times the Taylor polynomial of 2^-g (the table-driven scheme of Tang,
 // 1989), whose correction is added to the entry as a whole number.  log2(e) / t is

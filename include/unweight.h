@@ -614,7 +614,10 @@ typedef struct uw_sample_args {
  *     that id).  Logits of +infinity share all of the weight.  NaN in top_p or
  *     min_p: off; u is cut to [0, 1).
  *   - Weights are summed as whole multiples of 2^-40 of the largest one, so the
- *     sums are exact and the result is the same on every run.
+ *     sums are exact and the result is the same on every run.  Each weight is
+ *     right to 2^-29 of itself, or to that multiple: where the end of a prefix,
+ *     min_p or the choice lies nearer to its border, it may fall on the other
+ *     side.
  * vocab 1..262144; logits aligned to their type, row_stride >= vocab.  n_rows == 0 returns UW_OK and
  * launches nothing. */
 UW_API uw_status uw_sample(const uw_sample_args* a, void* stream);

@@ -167,3 +167,27 @@ def test_attention_reports_row_offsets_out_of_order(uw):
     # as far as the rows go, and requests without rows at their end: sound
     for fine in ([0, 2, 3, 46], [0, 2, 3, 3], [46, 46, 46, 46], [0, 0, 0, 0]):
         assert g._attend(uw, q, kc, vc, table, fine, kv)[2] == 0, fine
+
+
+@pytest.mark.parametrize("heat", [1.0, 0.3, 5.0])
+def test_sample_weights_to_what_is_stated(uw, heat):
+    """Rows of two logits whose second weight lies within 2^-27 of min_p (which is a float, so 2^-25 apart at most),
+    on either side: kept where it is larger, as long as the two are more than the stated 2^-29 apart.  (A table
+    entry and a correction are each rounded to half a unit of at least 2^30: 2^-30 together; the correction's FP32
+    steps, at most 2^-10 of the weight, add below 2^-32.)"""
+    import torch
+    rng, wide = np.random.default_rng(int(heat * 10)), np.longdouble
+    top = rng.choice(np.float32([0, 7.25, -31.0, 18.6]), 1 << 20)
+    low = (top - rng.uniform(0, 9, top.size) * heat).astype(np.float32)
+    w = np.exp((low.astype(wide) - top.astype(wide)) / wide(np.float32(heat)))
+    least = w.astype(np.float32)
+    off = (w / least.astype(wide) - 1).astype(np.float64)
+    rows = np.flatnonzero((np.abs(off) > 2.0**-29) & (np.abs(off) < 2.0**-27))[:60000]
+    assert rows.size > 10000 and (off[rows] > 0).mean() > 0.3 and (off[rows] < 0).mean() > 0.3
+    n = rows.size
+    x = torch.from_numpy(np.stack([top[rows], low[rows]], 1)).cuda()
+    # the last id that is kept: u is next to one, and its share is at least e^-9
+    ids, u = torch.full((n,), -9, dtype=torch.int64, device="cuda"), torch.full((n,), 1 - 2.0**-24, device="cuda")
+    uw.uw_sample(x, u, ids, temperature=torch.full((n,), heat, device="cuda"), min_p=torch.from_numpy(least[rows]).cuda())
+    wrong = np.flatnonzero((ids.cpu().numpy() == 1) != (off[rows] > 0))
+    assert wrong.size == 0, (wrong.size, np.log2(np.abs(off[rows][wrong])).tolist()[:9])
