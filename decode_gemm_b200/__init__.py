@@ -16,7 +16,6 @@ a status other than ``UW_OK``.
 from __future__ import annotations
 
 import ctypes as C
-import math
 import os
 import struct
 

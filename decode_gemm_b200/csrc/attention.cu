@@ -27,7 +27,6 @@
 //     for its copies and products in flight (once all warps have stopped: one that
 //     was through before the expiry has left some too), frees TMEM and returns.
 #include <cuda.h>
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -126,11 +125,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "=l"(reinterpret_cast<uint64_t&>(r))
       : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
   return r;
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // The weights 2^(x c - mc) of a row's 128 scores: BF16 into TMEM (they are the
@@ -411,8 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
     fail();
     return false;
   };
-  // Take unit n; false: no more (or aborted).  `leader`: this thread frees the
-  // descriptor (one per warp).
+  // Read unit n's descriptor once it is there; false: aborted.  (Each warp frees the descriptor itself.)
   const auto take = [&](uint32_t n, Unit* u) {
     const int i = n % kDescs;
     if (!wait(L::bDescFull + i, (n / kDescs) & 1)) return false;
@@ -544,10 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attention_kernel(const __gr
         if (u.n_tiles == 0) continue;
         // Q: the rows of (token, head) as they lie, one box per row tile and 64
         // values; units of one row tile take the two buffers in turn.  A single
-        // token comes alone, and the tile's other rows stay zero: the products
-        // are as long, but take less power, which bounds the clock of a long
-        // decoding run (seconds of the ragged batch: 367 us a call with the
-        // neighbouring tokens' rows in the tile, 357 so).
+        // token comes alone, and the tile's other rows stay as they are: zero in a
+        // batch of single tokens, else what the buffer's last longer unit left.
+        // With zeros the products are as long, but take less power, which bounds the
+        // clock of a long decoding run (seconds of the ragged batch: 367 us a call
+        // with the neighbouring tokens' rows in the tile, 357 so).
         for (int t = 0; t <= u.two && ok && !is_v; ++t) {
           const int buf = u.two ? t : (int)(pieces & 1);
           ok = __all_sync(0xFFFFFFFFu, wait(L::bQEmpty + buf, (q_used[buf] & 1) ^ 1));

@@ -1,7 +1,6 @@
 // The paged key/value cache around the attention: block tables and slot maps
 // from the requests' lengths (uw_paged_plan), and the norms and the rotation of
 // queries and keys in the pass that writes the cache (uw_qk_norm_rope).
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -240,10 +239,6 @@ struct RopeParams {
   int32_t page_shift;
 };
 
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

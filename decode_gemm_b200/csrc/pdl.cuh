@@ -5,8 +5,12 @@
 // A kernel launched with launch_pdl must call pdl_wait() before it touches any
 // memory an earlier kernel of the stream may write or read (inputs, workspace,
 // outputs, hand-off flags); it calls pdl_release() once its own CTAs no longer
-// need to hold back the next kernel's start (here: right after set-up, since
-// every kernel of the library is a persistent grid of at most one CTA per SM).
+// need to hold back the next kernel's start.  Here that is right behind
+// pdl_wait(): the next kernel starts once every CTA of this one has called it
+// or ended, so where a grid is larger than what fits the GPU at a time (norms and
+// rotation, sampling, the attention's join) not before its last CTAs have begun,
+// and it takes nothing that this one's CTAs still need.  Since every kernel waits,
+// all before it have ended and are visible when pdl_wait() returns.
 #pragma once
 
 #include <cuda_runtime.h>

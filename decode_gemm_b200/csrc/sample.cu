@@ -379,10 +379,6 @@ struct Row {
       for (int j = 0; j < V; ++j) f(x[j], e + j);
     });
   }
-  template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-    each_raw([&](float x, int e) { f(clean(x), e); });
-  }
 
   __device__ __forceinline__ void sync_cluster() const {
     if (ranks > 1) cluster_sync();

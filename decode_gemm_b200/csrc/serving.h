@@ -2,6 +2,7 @@
 // host-side checks of their arguments and the device they run on.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -30,6 +31,12 @@ inline uw_status device_of(const void* p, int* dev) {
   if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return UW_ERR_ARG;
   *dev = at.device;
   return UW_OK;
+}
+
+// Two BF16 values, rounded to nearest even, as they lie in memory.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Multiprocessors of a device, asked for once per device.
