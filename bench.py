@@ -61,9 +61,9 @@ NOMINAL_HBM_GBS = 7700.0  # B200 HBM3e, nominal (HGX)
 # dram__bytes_write.sum of one launch), valid only while the kernel source
 # (src_sha, see _kernel_src_sha) is unchanged.
 TRAFFIC = {
-    "gemm_palette": {"bytes_per_launch": 89.744128e6 + 2.605312e6, "src_sha": "0bd3631b51fba772",
+    "gemm_palette": {"bytes_per_launch": 89.630976e6 + 2.463488e6, "src_sha": "47b8a394648c0901",
                      "capture": "palette GEMM, 14336x4096, M = 1 launch"},
-    "decode_full": {"bytes_per_launch": 87.415040e6 + 64.024064e6, "src_sha": "2a78f2d845afbc82",
+    "decode_full": {"bytes_per_launch": 87.109376e6 + 63.757568e6, "src_sha": "c59bd366e353c7ee",
                     "capture": "full decode, 14336x4096 (output partly still in L2)"},
 }
 

@@ -48,11 +48,11 @@
 
 #include <cstdlib>
 #include <cstring>
-#include <mutex>
 
 #include "bf16_fields.cuh"
 #include "gemm_sm100.cuh"
 #include "pdl.cuh"
+#include "tma_map.h"
 #include "uw_kernels.h"
 
 namespace uw {
@@ -1125,25 +1125,6 @@ __global__ void __launch_bounds__(threads_for(MODE), 1)
 
 // ----------------------------------------------------------------- host ----
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const void* base,
                  uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swizzle) {
@@ -1456,7 +1437,7 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t s, const LaunchHooks* ho
           if (clusters < 1) return cudaErrorInvalidConfiguration;
           if (G2 > 2 * clusters) G2 = 2 * clusters;
         }
-        e = launch_pdl_pair(gemm_kernel<kGemmBf16, 1, true>, G2, threads_for(kGemmBf16), smem, s, p);
+        e = launch_pdl_cluster(gemm_kernel<kGemmBf16, 1, true>, G2, 2, threads_for(kGemmBf16), smem, s, p);
       } else {
         if ((e = set_smem_attr<kGemmBf16, 1>()) != cudaSuccess) return e;
         e = launch_pdl(gemm_kernel<kGemmBf16, 1>, G, threads_for(kGemmBf16), smem, s, p);
