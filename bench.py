@@ -63,7 +63,7 @@ NOMINAL_HBM_GBS = 7700.0  # B200 HBM3e, nominal (HGX)
 TRAFFIC = {
     "gemm_palette": {"bytes_per_launch": 89.630976e6 + 2.463488e6, "src_sha": "47b8a394648c0901",
                      "capture": "palette GEMM, 14336x4096, M = 1 launch"},
-    "decode_full": {"bytes_per_launch": 87.109376e6 + 63.757568e6, "src_sha": "c59bd366e353c7ee",
+    "decode_full": {"bytes_per_launch": 87.216640e6 + 63.729408e6, "src_sha": "91bbe046dc09bcfc",
                     "capture": "full decode, 14336x4096 (output partly still in L2)"},
 }
 

@@ -789,9 +789,12 @@ __global__ void __launch_bounds__(32 * (MODE == kDecodeDot ? kDotMaxWarps : kMax
   }
 }
 
+// (The limit belongs to the kernel and the device, not to one launch: always that of the widest launch, so
+// that no other thread's call lowers it before this one's launch.)
 template <typename F>
-cudaError_t set_attrs(F* f, size_t smem) {
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t set_attrs(F* f, size_t smem, int mode) {
+  const size_t most = smem_bytes(mode == kDecodeDot ? kDotMaxWarps : kMaxWarps, mode);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   // the smallest shared-memory split that holds the CTA leaves L1 the rest
   const int pct = (int)((100 * (smem + 1024) + 228 * 1024 - 1) / (228 * 1024));
   if (e == cudaSuccess)
@@ -870,30 +873,30 @@ cudaError_t launch_decode(int mode, const DecodeArgs& a, void* out, int ctas, cu
       if (a.rows || !a.x || !a.y || !a.part || !a.row_cnt || a.m < 1 || a.m > kDotMaxM ||
           a.run < 1 || a.cpr % a.run)
         return cudaErrorInvalidValue;
-      e = set_attrs(decode_kernel<kDecodeDot, false>, smem);
+      e = set_attrs(decode_kernel<kDecodeDot, false>, smem, mode);
       if (e == cudaSuccess)
         e = launch_pdl(decode_kernel<kDecodeDot, false>, grid, block, smem, s, a, out);
       break;
     }
     case kDecodeExp:
       if (a.rows) return cudaErrorInvalidValue;
-      e = set_attrs(decode_kernel<kDecodeExp, false>, smem);
+      e = set_attrs(decode_kernel<kDecodeExp, false>, smem, mode);
       if (e == cudaSuccess) e = launch_pdl(decode_kernel<kDecodeExp, false>, grid, block, smem, s, a, out);
       break;
     case kDecodeFull:
       if (a.rows) {
-        e = set_attrs(decode_kernel<kDecodeFull, true>, smem);
+        e = set_attrs(decode_kernel<kDecodeFull, true>, smem, mode);
         if (e == cudaSuccess)
           e = launch_pdl(decode_kernel<kDecodeFull, true>, grid, block, smem, s, a, out);
       } else {
-        e = set_attrs(decode_kernel<kDecodeFull, false>, smem);
+        e = set_attrs(decode_kernel<kDecodeFull, false>, smem, mode);
         if (e == cudaSuccess)
           e = launch_pdl(decode_kernel<kDecodeFull, false>, grid, block, smem, s, a, out);
       }
       break;
     case kDecodePalette:
       if (a.rows) return cudaErrorInvalidValue;
-      e = set_attrs(decode_kernel<kDecodePalette, false>, smem);
+      e = set_attrs(decode_kernel<kDecodePalette, false>, smem, mode);
       if (e == cudaSuccess) e = launch_pdl(decode_kernel<kDecodePalette, false>, grid, block, smem, s, a, out);
       break;
     default:
