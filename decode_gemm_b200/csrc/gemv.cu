@@ -401,6 +401,8 @@ size_t gemv_smem_for(int mode, int rows, int segs, int mm, int kbk) {
                             : gemv_smem<kGemmPalette>(rows, segs, mm, kbk);
 }
 
+constexpr size_t kGvSmemLimit = 227 * 1024;  // of dynamic shared memory; the kernels have no other
+
 bool gemv_supported(const GemmArgs& a) {
   if (a.M < 1 || a.M > kGemvMaxM || a.N < 1 || a.K < 64 || a.K % 64) return false;
   int dev = 0, sms = 148;
@@ -409,7 +411,7 @@ bool gemv_supported(const GemmArgs& a) {
   const int64_t segs = (a.K + kSeg - 1) / kSeg;
   const int64_t rows = (a.N + sms - 1) / sms;
   if (rows * segs >= (int64_t)1 << 30) return false;
-  return gemv_smem_for(a.mode, (int)rows, (int)segs, kGemvMaxM, (int)(a.K / 64)) <= 227 * 1024;
+  return gemv_smem_for(a.mode, (int)rows, (int)segs, kGemvMaxM, (int)(a.K / 64)) <= kGvSmemLimit;
 }
 
 cudaError_t launch_gemv(const GemmArgs& a, cudaStream_t s, const LaunchHooks* hooks) {
@@ -455,9 +457,9 @@ cudaError_t launch_gemv(const GemmArgs& a, cudaStream_t s, const LaunchHooks* ho
   const int kind = a.mode == kGemmBf16 ? 7 : (a.mode == kGemmExp ? 8 : 9);
   const int slot = hooks && hooks->begin ? hooks->begin(hooks->ctx, kind) : -1;
   auto go = [&](auto kernel) {
-    cudaError_t r = cudaSuccess;
-    if (smem > 48 * 1024)
-      r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the kernel's limit, not this launch's: always the most that any may ask for, so that no other
+    // thread's call lowers it before the launch)
+    cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGvSmemLimit);
     if (r == cudaSuccess) r = launch_pdl(kernel, dim3((unsigned)blocks), dim3(kGvThreads), smem, s, p);
     return r;
   };
