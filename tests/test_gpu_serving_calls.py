@@ -191,3 +191,53 @@ def test_sample_weights_to_what_is_stated(uw, heat):
     uw.uw_sample(x, u, ids, temperature=torch.full((n,), heat, device="cuda"), min_p=torch.from_numpy(least[rows]).cuda())
     wrong = np.flatnonzero((ids.cpu().numpy() == 1) != (off[rows] > 0))
     assert wrong.size == 0, (wrong.size, np.log2(np.abs(off[rows][wrong])).tolist()[:9])
+
+
+def test_calls_at_once_on_streams_and_in_graphs(uw):
+    """Calls that share nothing, on a stream each, eager and as replayed graphs: what each gives alone."""
+    import torch
+    from tests import test_gpu_serving as g
+    gen, rng = g._gen(40), np.random.default_rng(40)
+    pieces = []
+    for lens, heads, kv_heads, dim, window in (([(3000, 1), (70, 70), (0, 0), (5, 9)], 8, 2, 128, 0),
+                                               ([(900, 300), (260, 1)], 6, 3, 64, 100), ([(40, 1)] * 200, 4, 4, 128, 0)):
+        q, kc, vc, table, cu, kv = g._requests(gen, rng, lens, 16, heads, kv_heads, dim)
+        t, c, l, out = g._ints(table), g._ints(cu), g._ints(kv), torch.zeros_like(q)
+        ws = torch.empty(uw.uw_paged_attention_workspace_bytes(heads, kv_heads, dim), dtype=torch.uint8, device="cuda")
+        pieces.append((out, lambda q=q, kc=kc, vc=vc, t=t, c=c, l=l, out=out, ws=ws, w=window:
+                       uw.uw_paged_attention(q, kc, vc, t, c, l, out, window=w, ws=ws)))
+    for rows, vocab in ((1, 131072), (200, 5003)):
+        x, u, ids = torch.randn((rows, vocab), generator=gen, device="cuda") * 3, torch.rand(rows, generator=gen, device="cuda"), \
+            torch.zeros(rows, dtype=torch.int64, device="cuda")
+        p = torch.full((rows,), 0.95, device="cuda")
+        pieces.append((ids, lambda x=x, u=u, ids=ids, p=p: uw.uw_sample(x, u, ids, top_p=p)))
+    t, args = _plan_tensors(3500)
+    plan = args(uw)
+    pieces.append((t["slots"], lambda: uw._check(uw.lib.uw_paged_plan(C.byref(plan), torch.cuda.current_stream().cuda_stream), "plan")))
+    want = []
+    for out, call in pieces:
+        call()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    streams = [torch.cuda.Stream() for _ in pieces]
+    graphs = []
+    for out, call in pieces:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for graphed in (False, True):
+        for out, _ in pieces:
+            out.zero_()
+        torch.cuda.synchronize()
+        for i in range(20):
+            for j, ((_, call), graph) in enumerate(zip(pieces, graphs)):
+                with torch.cuda.stream(streams[(i + j) % len(pieces) if graphed and i % 5 == 0 else j]):
+                    if graphed:
+                        graph.replay()
+                    else:
+                        call()
+            if graphed and i % 5 in (4, 0):  # (a graph moves to another stream only once its last run is over)
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        for k, ((out, _), w) in enumerate(zip(pieces, want)):
+            assert torch.equal(out, w), (k, graphed)
