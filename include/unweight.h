@@ -497,6 +497,8 @@ typedef struct uw_paged_plan_args {
  *   - A token that falls on a held page with a negative id gets slot -1, with
  *     UW_FLAG_BAD_INPUT.
  *   - kv_len may be ctx_len's array, and head_out head_in's (a loop's state).
+ *     A refused request's length is then lost with its kv_len of 0: a caller who
+ *     means to try it again keeps the length elsewhere.
  * n_requests 0..8192 (0: UW_OK, only padding rows and head_out are written),
  * page_size 1..1024, a power of two; n_rows 0..2^30. */
 UW_API uw_status uw_paged_plan(const uw_paged_plan_args* a, void* stream);
@@ -524,11 +526,12 @@ typedef struct uw_qk_norm_rope_args {
  * by the angle positions[row] * inv_freq[i]: (a, b) -> (a cos - b sin,
  * b cos + a sin).  Pair i is (i, i + rot_dim / 2), or (2i, 2i + 1) when
  * interleaved is nonzero.  Queries go to q_out, keys to the cache's slot
- * slots[row], and v's rows unchanged to the same slot; a slot named by
- * two rows gets one of them, which may differ from head to head.  Sums, angles (64 bits) and rotation are not rounded
- * before the result is (to nearest even).  Every row gets its q_out; a row with
- * slot -1 stores nothing, and one with a slot outside the cache stores nothing
- * and raises UW_FLAG_BAD_INPUT.
+ * slots[row], and v's rows unchanged to the same slot; a slot named by two rows
+ * gets one of them, which may differ from head to head.  Sums, angles (64 bits)
+ * and rotation are not rounded before the result is (to nearest even);
+ * mean(x^2) is held in FP32, so heads with values beyond about 2^60 leave its
+ * range.  Every row gets its q_out; a row with slot -1 stores nothing, and one
+ * with a slot outside the cache stores nothing and raises UW_FLAG_BAD_INPUT.
  * head_dim a multiple of 16, 16..256; rot_dim a multiple of 16, 0..head_dim;
  * heads of a row are head_dim apart; row strides multiples of 8 and pointers
  * 16-byte aligned.  q_out may be q's own array (same stride).  n_rows == 0
@@ -576,9 +579,10 @@ typedef struct uw_paged_attention_args {
  *   - Results do not depend on what ran before, and are bitwise repeatable;
  *     their rounding depends on the whole batch (it decides where the work of a
  *     request is divided between CTAs).
- * head_dim 64 or 128 (UW_ERR_UNSUPPORTED otherwise); n_heads / n_kv_heads at
- * most 128; n_requests 0..8192; window below 2^30 (or beyond the table); pointers 16-byte aligned, strides multiples of
- * 8.  ws_dev: at least uw_paged_attention_workspace_bytes, 256-byte aligned;
+ * head_dim 64 or 128 (UW_ERR_UNSUPPORTED otherwise, also for the other sizes
+ * that uw_qk_norm_rope stores); n_heads / n_kv_heads at most 128; n_requests
+ * 0..8192; window below 2^30 (or beyond the table); pointers 16-byte aligned,
+ * strides multiples of 8.  ws_dev: at least uw_paged_attention_workspace_bytes, 256-byte aligned;
  * its contents mean nothing between calls, but two calls that share one must
  * not overlap on the GPU (two graphs captured with one included). */
 UW_API uw_status uw_paged_attention_workspace_bytes(int32_t n_heads, int32_t n_kv_heads,
@@ -618,8 +622,8 @@ typedef struct uw_sample_args {
  *     right to 2^-29 of itself, or to that multiple: where the end of a prefix,
  *     min_p or the choice lies nearer to its border, it may fall on the other
  *     side.
- * vocab 1..262144; logits aligned to their type, row_stride >= vocab.  n_rows == 0 returns UW_OK and
- * launches nothing. */
+ * vocab 1..262144; logits aligned to their type, row_stride >= vocab.
+ * n_rows == 0 returns UW_OK and launches nothing. */
 UW_API uw_status uw_sample(const uw_sample_args* a, void* stream);
 
 /* Synchronise the handle's stream, then return and clear the device status
