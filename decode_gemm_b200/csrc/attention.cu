@@ -127,9 +127,11 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
-// The weights 2^(x c - mc) of a row's 128 scores: BF16 into TMEM (they are the
-// product's operand; that rounding, at most 2^-8 of each, is the only one
-// beside FP32's), their FP32 sum returned.
+// The weights 2^(x c - mc) of a row's 128 scores: BF16 into TMEM, their FP32 sum
+// returned.  They are the product's operand, whose type V's is; that rounding, at
+// most 2^-8 of each, is the only one beside FP32's.  It takes the root mean square
+// error of a BF16 output from 0.0017 of its size, its own rounding, to 0.0020 to
+// 0.0023.  Weights in two parts would be exact to 2^-16, for twice the product.
 __device__ __forceinline__ float exponentials(const uint32_t (&x)[kKeys], float c, float mc, uint32_t to) {
   const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
