@@ -241,3 +241,24 @@ def test_calls_at_once_on_streams_and_in_graphs(uw):
         torch.cuda.synchronize()
         for k, ((out, _), w) in enumerate(zip(pieces, want)):
             assert torch.equal(out, w), (k, graphed)
+
+
+def test_attention_keeps_bad_queries_to_their_rows(uw):
+    """NaN and infinities in one row's query, and in rows of no request: every other row is bitwise as before."""
+    import torch
+    from tests import test_gpu_serving as g
+    gen, rng = g._gen(50), np.random.default_rng(50)
+    for heads, kv_heads, dim, window in ((8, 2, 128, 0), (6, 6, 64, 90), (16, 1, 128, 0)):
+        q, kc, vc, table, cu, kv = g._requests(gen, rng, [(700, 300), (9, 1), (40, 1), (2000, 3), (0, 0)], 16, heads, kv_heads, dim)
+        clean = g._attend(uw, q, kc, vc, table, cu, kv, window=window)
+        last = int(cu[-1])
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            rows = [0, 17, 299, 300, int(cu[3]) + 1]
+            spoilt = q.clone()
+            spoilt[rows] = bad
+            spoilt[last:] = bad
+            out, lse, flag = g._attend(uw, spoilt, kc, vc, table, cu, kv, window=window)
+            others = [r for r in range(q.shape[0]) if r not in rows]
+            assert flag == 0
+            assert torch.equal(out[others], clean[0][others]) and torch.equal(lse[others], clean[1][others]), (heads, bad)
+            assert bool(torch.isnan(out[rows]).all()), (heads, bad)
